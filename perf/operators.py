@@ -357,24 +357,17 @@ def _plain_verify(st):
 
 # ---------------------------------------------------------------------------------- one pass
 
-def _handle(D, state, k, v):
-    """The library's handle of the state's cache, which a program keeps as long as the cache."""
-    if "handle" not in state:
-        state["handle"] = D.KV4Cache.of(state[k], state[v], state["c"]["hd"])
-    return state["handle"]
-
-
 def run(state):
     c = state["c"]
     if not own:
         return globals()["_plain_" + c["op"]](state)
     from speculative_block_drafter_gb300 import drafter as D
     if c["op"] == "attend":
-        cache = _handle(D, state, "k", "v")
+        cache = D.KV4Cache.of(state["k"], state["v"], c["hd"])
         return cache.attend(state["q"], state["lo"], state["hi"], state["anchor"], window=c["window"],
                             causal=c["causal"])
     if c["op"] == "write":
-        cache = _handle(D, state, "ck", "cv")
+        cache = D.KV4Cache.of(state["ck"], state["cv"], c["hd"])
         cache.write(state["at"], state["k"], state["v"])
         return cache.read(state["at"], c["n"])
     if c["op"] == "select":
