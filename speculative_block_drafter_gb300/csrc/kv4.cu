@@ -304,7 +304,9 @@ __device__ __forceinline__ void a4_pack(float p0, float p1, uint32_t &hi, uint32
 }
 // The power of two f0 * f1 that brings a row's largest magnitude to [2^10, 2^11)
 // (1 for a row of zeros or one that is not finite), and the factor from a product
-// with the row so scaled to a score in the base-2 domain.
+// with the row so scaled to a score in the base-2 domain: above 0, as masks of -inf are
+// multiplied by it. (Where it would leave f32's normal range, scores are far below any
+// step of a weight: products are below 2^33.)
 __device__ __forceinline__ float a4_row_scale(float amax, float scale, float &f0, float &f1) {
   int ex = 0;
   if (amax > 0.f && amax < INFINITY) {
@@ -313,7 +315,9 @@ __device__ __forceinline__ float a4_row_scale(float amax, float scale, float &f0
   }
   f0 = __int_as_float((127 + ex / 2) << 23);
   f1 = __int_as_float((127 + ex - ex / 2) << 23);
-  return scale * 1.4426950408889634f * __int_as_float((127 - ex / 2) << 23) * __int_as_float((127 - (ex - ex / 2)) << 23);
+  return fmaxf(scale * 1.4426950408889634f * __int_as_float((127 - ex / 2) << 23) *
+                   __int_as_float((127 - (ex - ex / 2)) << 23),
+               1.17549435e-38f);
 }
 // N values of a query row, STEP apart (f32 rows with SPL = 2, f16 or bf16 ones else).
 template <int SPL, int N, int STEP>
