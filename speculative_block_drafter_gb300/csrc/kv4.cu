@@ -198,6 +198,7 @@ __global__ void __launch_bounds__(256) k_kv4_read(const __grid_constant__ Kv4Seq
 // of splits a pair, 32 blocks over 8,192 rows each took 190 us and not 153: the last
 // CTAs of a launch had the GPU to themselves.)
 constexpr float A4_TAU = 11.f, A4_BIAS = 4.f;
+constexpr float A4_NONE = 3.402823466e38f;  // minus the reference of a query that has seen no row
 
 struct A4Seq {
   const uint8_t *k, *v;    // the caches
@@ -334,6 +335,20 @@ __device__ __forceinline__ void a4_row(const A4Args &A, int64_t at, float (&x)[N
       x[e] = A.dtype == DFLASH_F16 ? __half2float(__ushort_as_half(w[e])) : __uint_as_float((uint32_t)w[e] << 16);
   }
 }
+// Minus the reference for a query whose largest score is y (base 2). From 2^24 on, where
+// a score's rounding passes 1, the reference is a few of its steps lower still: the
+// product's rest, which a fused sum with the reference leaves, then never takes the
+// largest score's weight away. (At the cap: y is infinite.)
+__device__ __forceinline__ float a4_ref(float y) {
+  return fabsf(y) >= 16777216.f ? A4_BIAS - y + fminf(fabsf(y) * 0x1p-22f, 1e32f) : A4_BIAS - y;
+}
+// A score against its new reference, kept inside f16's range as a weight where those
+// steps pass it (an ordinary one is never above TAU there).
+__device__ __forceinline__ float a4_capped(float x) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(A4_TAU));
+  return r;
+}
 // The larger of two values, NaN when one is.
 __device__ __forceinline__ float a4_max(float a, float b) {
   float r;
@@ -379,7 +394,7 @@ __device__ __forceinline__ float a4_max(float a, float b) {
 // far less BIAS), so that P stays below 2^(TAU + BIAS) in f16. Scores are per
 // key, so finding a new reference reduces over lanes; a chunk in which no score
 // passes costs one barrier with a vote. A query that has seen no row yet has
-// the reference -1e30, which any score passes. A score that is not a number
+// f32's lowest number as its reference, which any score passes. A score that is not a number
 // passes too and makes its query's reference, and so its output, NaN.
 template <int HD, int NQ, int SPL>
 struct A4 {
@@ -634,7 +649,7 @@ __global__ void __launch_bounds__(A4<HD, NQ, SPL>::THREADS, 1) k_attn4(const __g
       float l[QPT];
 #pragma unroll
       for (int i = 0; i < QPT; ++i) l[i] = 0.f;
-      if (lane < QPT) nm[lane] = 1e30f;
+      if (lane < QPT) nm[lane] = A4_NONE;
       if (nch > 0) {
         stage_q(job);  // (the scores of the piece before, the last ones' last readers, are done)
         warp_arrive(qfull);
@@ -732,8 +747,9 @@ __global__ void __launch_bounds__(A4<HD, NQ, SPL>::THREADS, 1) k_attn4(const __g
           auto moved = [&](int e, float old) {
             const float4 v = *(const float4 *)ev4[e];
             const float y = a4_max(a4_max(v.x, v.y), a4_max(v.z, v.w));
-            if (old == 1e30f) return y != -INFINITY ? A4_BIAS - y : old;
-            return y + old > A4_TAU ? A4_BIAS - y : old;
+            const float nn = a4_ref(y);
+            if (old == A4_NONE) return y != -INFINITY ? nn : old;
+            return y + old > A4_TAU && nn < old ? nn : old;  // (never back down)
           };
           if (i > 0) {
             // l and O of the chunks before, whose products are done (chunk j - 2's first:
@@ -746,7 +762,7 @@ __global__ void __launch_bounds__(A4<HD, NQ, SPL>::THREADS, 1) k_attn4(const __g
 #pragma unroll
             for (int e = 0; e < QPT; ++e) {
               const float old = nm[e], nn = moved(e, old);
-              alpha[e] = old == 1e30f || nn == old ? 1.f : a4_ex2(nn - old);
+              alpha[e] = old == A4_NONE || nn == old ? 1.f : a4_ex2(nn - old);
               l[e] *= alpha[e];
               any = any || alpha[e] != 1.f;
             }
@@ -787,6 +803,8 @@ __global__ void __launch_bounds__(A4<HD, NQ, SPL>::THREADS, 1) k_attn4(const __g
           } else {
             scores(false);
           }
+#pragma unroll
+          for (int e = 0; e < QPT; ++e) t[e] = a4_capped(t[e]);
         }
         tc_fence_before();
         warp_arrive(sfree + 8 * sb);
@@ -856,7 +874,7 @@ __global__ void __launch_bounds__(A4<HD, NQ, SPL>::THREADS, 1) k_attn4(const __g
       const int d = key;  // this thread's dimension of O
       const bool stat = (warp & 3) == 0 && lane < QPT && q0 + lane < Q;  // this lane writes query q0 + lane's statistics
       float m = -INFINITY, L = 0.f;
-      if (stat && have && nm[lane] != 1e30f) {
+      if (stat && have && nm[lane] != A4_NONE) {
         const float4 s = *(const float4 *)lsum[q0 + lane];
         m = -nm[lane];
         L = s.x + s.y + s.z + s.w;
@@ -885,7 +903,7 @@ __global__ void __launch_bounds__(A4<HD, NQ, SPL>::THREADS, 1) k_attn4(const __g
           for (int i = 0; i < QPT; ++i) {
             const float4 s = *(const float4 *)lsum[q0 + i];
             // a query that sees no row: 0
-            const float inv = have && nm[i] != 1e30f ? 1.f / (s.x + s.y + s.z + s.w) : 0.f;
+            const float inv = have && nm[i] != A4_NONE ? 1.f / (s.x + s.y + s.z + s.w) : 0.f;
             if (q0 + i < Q) st_elem(A.y, (row0 + (int64_t)r * A.heads + hr) * HD + d, A.dtype, o[i] * inv);
             if (++r == R) {
               r = 0;
@@ -1240,7 +1258,7 @@ __global__ void __launch_bounds__(Few<HD>::THREADS, few_ctas(NT)) k_attn4_few(co
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[i][nt][e] = 0.f;
       l[nt][0] = l[nt][1] = 0.f;
-      negm[nt][0] = negm[nt][1] = 1e30f;               // no row seen yet
+      negm[nt][0] = negm[nt][1] = A4_NONE;               // no row seen yet
     }
     constexpr int KC = HD == 128 ? 1 : 2, VC = HD == 128 ? 2 : 4;  // threads that share a group of 32 values
     const uint32_t kr = ring32 + t / KC * F::KG + krow * 16 + t % KC * 8;
@@ -1340,12 +1358,13 @@ __global__ void __launch_bounds__(Few<HD>::THREADS, few_ctas(NT)) k_attn4_few(co
 #pragma unroll
             for (int f = 4; f < 32; f <<= 1) y = a4_max(y, __shfl_xor_sync(0xffffffffu, y, f));
             const float nm = negm[nt][e];
+            const float nn = a4_ref(y);
             float al = 1.f;
-            if (nm == 1e30f) {
-              if (y != -INFINITY) negm[nt][e] = A4_BIAS - y;
-            } else if (!(y + nm <= A4_TAU)) {
-              negm[nt][e] = A4_BIAS - y;
-              al = a4_ex2(negm[nt][e] - nm);
+            if (nm == A4_NONE) {
+              if (y != -INFINITY) negm[nt][e] = nn;
+            } else if (!(y + nm <= A4_TAU) && !(nn >= nm)) {  // (never back down)
+              negm[nt][e] = nn;
+              al = a4_ex2(nn - nm);
             }
             l[nt][e] *= al;
 #pragma unroll
@@ -1354,7 +1373,7 @@ __global__ void __launch_bounds__(Few<HD>::THREADS, few_ctas(NT)) k_attn4_few(co
               o[i][nt][2 + e] *= al;
             }
 #pragma unroll
-            for (int k = e; k < 4; k += 2) x[nt][k] = fmaf(c[nt][k], sl2[nt][e], negm[nt][e]);
+            for (int k = e; k < 4; k += 2) x[nt][k] = a4_capped(fmaf(c[nt][k], sl2[nt][e], negm[nt][e]));
           }
       }
       uint32_t pf[NT][SPL][2];
@@ -1429,7 +1448,7 @@ __global__ void __launch_bounds__(Few<HD>::THREADS, few_ctas(NT)) k_attn4_few(co
         for (int f = 4; f < 32; f <<= 1) x += __shfl_xor_sync(0xffffffffu, x, f);
         const int q = 8 * nt + 2 * t + e;
         if (g == 0) {
-          wm[warp][q] = negm[nt][e] == 1e30f ? -INFINITY : -negm[nt][e];
+          wm[warp][q] = negm[nt][e] == A4_NONE ? -INFINITY : -negm[nt][e];
           wl[warp][q] = x;
         }
 #pragma unroll
