@@ -192,13 +192,20 @@ __global__ void __launch_bounds__(256) k_kv4_read(const __grid_constant__ Kv4Seq
 // The context rows of all (sequence, KV head) pairs, in rounds of 128 rows, are
 // shared out evenly over the CTAs of a launch, whatever the sequences' lengths:
 // a CTA takes the next T / G or one more of them, pieces of one or more pairs. A piece
-// that is its whole pair gives y; the others leave a partial (unnormalised o,
+// that is its whole pair in one run gives y; the others leave a partial (unnormalised o,
 // reference m, sum l per query) in slot i + (index of the pair), which is different
 // for every piece, and a second kernel merges a pair's partials. (With a fixed number
 // of splits a pair, 32 blocks over 8,192 rows each took 190 us and not 153: the last
 // CTAs of a launch had the GPU to themselves.)
 constexpr float A4_TAU = 11.f, A4_BIAS = 4.f;
 constexpr float A4_NONE = 3.402823466e38f;  // minus the reference of a query that has seen no row
+
+// A matrix instruction cuts off what its f32 sum does not hold, always towards 0, so that
+// a sum of n / 16 steps drifts by some 2^-23 of itself a step (3e-4 after 32,768 rows). A
+// long piece is therefore taken in runs of at most 256 steps of a sum, whose results are
+// joined in ordinary f32 in the piece's slot. (A run's end and the next one's start cost
+// k_attn4 about 2.5 us: 32 blocks over 32,768 rows each 533 us, in one run a piece 516.)
+constexpr int A4_STEPS = 256;
 
 struct A4Seq {
   const uint8_t *k, *v;    // the caches
@@ -220,8 +227,10 @@ struct A4Args {
   int always_part;         // partials of whole pairs too (the merge packs them)
   float scale;
   int64_t round0[MAX_BATCH + 1];  // the first round of sequence b's pairs
+  int64_t run0[MAX_BATCH + 1];    // the first run of sequence b's pairs
   int64_t share;           // rounds of a CTA, at least
   int batch, ctas, more;
+  int run;                 // rounds of a run
 };
 
 // Rounds of a pair. k_attn4's are the tiles its range touches and the own rows'
@@ -238,6 +247,7 @@ __host__ __device__ __forceinline__ int a4_rounds(const A4Seq &s) {
   const int groups = (s.n > 0 ? (int)(((int64_t)first + s.n + 15) / 16) - first / 16 : 0) + (s.ok ? 1 : 0);
   return groups > 8 ? (groups + 7) / 8 : 1;
 }
+__host__ __device__ __forceinline__ int a4_runs(const A4Args &A, int nr) { return (nr + A.run - 1) / A.run; }
 // The first round of CTA i (of them, `more` take one round more than the others);
 // the CTA that takes round t.
 __device__ __forceinline__ int64_t a4_first(const A4Args &A, int64_t i) { return i * A.share + min(i, (int64_t)A.more); }
@@ -246,12 +256,12 @@ __device__ __forceinline__ int64_t a4_cta(const A4Args &A, int64_t t) {
   return t < big ? a4_div(t, A.share + 1) : A.more + a4_div(t - big, A.share);
 }
 
-// A CTA's pieces, one after another.
+// A CTA's pieces, one after another, run by run.
 template <bool FEW>
 struct A4Piece {
   int64_t rnd, rend;  // rounds still to take
   int b, h;           // the piece's pair
-  int r0, r1, nr;     // its rounds [r0, r1) of the pair's nr
+  int r0, r1, nr;     // the run's rounds [r0, r1) of the pair's nr
   __device__ __forceinline__ void start(const A4Args &A) {
     rnd = a4_first(A, blockIdx.x);
     rend = a4_first(A, (int64_t)blockIdx.x + 1);
@@ -264,11 +274,18 @@ struct A4Piece {
     const int64_t in_seq = rnd - A.round0[b];
     h = (int)a4_div(in_seq, nr);
     r0 = (int)(in_seq - (int64_t)h * nr);
-    r1 = (int)min((int64_t)nr, r0 + (rend - rnd));
+    r1 = (int)min((int64_t)nr, r0 + min(rend - rnd, (int64_t)A4_STEPS));
     rnd += r1 - r0;
     return true;
   }
-  __device__ __forceinline__ bool whole(const A4Args &A) const { return r0 == 0 && r1 == nr && !A.always_part; }
+  // The piece's first round (of which the CTA's first piece may not be the pair's), and
+  // how many of its runs are still to come.
+  __device__ __forceinline__ int begin(const A4Args &A) const {
+    return (int)max((int64_t)0, a4_first(A, blockIdx.x) - (rnd - r1));
+  }
+  __device__ __forceinline__ int left() const {
+    return (int)((min((int64_t)nr - r1, rend - rnd) + A4_STEPS - 1) / A4_STEPS);
+  }
   __device__ __forceinline__ int64_t slot(const A4Args &A) const { return (int64_t)blockIdx.x + (int64_t)b * A.kv + h; }
 };
 // The rows of sequence s's range that every query sees.
@@ -456,34 +473,40 @@ __device__ __forceinline__ void tmem_st_n(uint32_t addr, const uint32_t (&r)[N])
   }
 }
 
-// A piece as the warps of k_attn4 read it from shared memory: its first chunk's
+// A run of a piece as the warps of k_attn4 read it from shared memory: its first chunk's
 // tiles and row of the range, its chunks (the last one the own rows' with `own`).
 struct __align__(16) A4Job {
   const uint8_t *k, *v, *ok, *ov;
   int64_t slot;
   int b, h, nch, lo, n, own, whole;
+  int prior, left;  // the piece's runs before (are there any) and behind it
 };
-constexpr int A4_JOBS = 16;  // pieces a window holds
+constexpr int A4_JOBS = 16;  // runs a window holds
 
-// Piece `i` (counted from the CTA's first) into *job; false past the last one.
+// Run `i` (counted from the CTA's first) into *job; false past the last one. A pair's runs
+// lie at multiples of A.run rounds from its start; a CTA's first and last may be parts.
 template <int HD>
 __device__ __forceinline__ bool a4_job(const A4Args &A, int64_t i, A4Job *job) {
   const int64_t r0 = a4_first(A, blockIdx.x), r1 = a4_first(A, (int64_t)blockIdx.x + 1);
-  // the pair that holds round r0, and the one i further on
+  // the run that holds round r0, and the one i further on
   int b = 0;
   while (r0 >= A.round0[b + 1]) ++b;
   int nr = a4_rounds<false>(A.seq[b]);
-  const int64_t pair = (int64_t)b * A.kv + a4_div(r0 - A.round0[b], nr) + i;
-  b = (int)a4_div(pair, A.kv);
+  const int64_t in_seq = r0 - A.round0[b], h0 = a4_div(in_seq, nr);
+  int64_t u = A.run0[b] + h0 * a4_runs(A, nr) + (int)(in_seq - h0 * nr) / A.run + i;
+  while (b < A.batch && u >= A.run0[b + 1]) ++b;
   if (b >= A.batch) return false;
   const A4Seq &s = A.seq[b];
   nr = a4_rounds<false>(s);
-  const int h = (int)(pair - (int64_t)b * A.kv);
+  u -= A.run0[b];
+  const int h = (int)a4_div(u, a4_runs(A, nr)), run = (int)(u - (int64_t)h * a4_runs(A, nr));
   const int64_t t0 = A.round0[b] + (int64_t)h * nr;
-  const int64_t f = max((int64_t)0, r0 - t0), e = min((int64_t)nr, r1 - t0);
+  // the piece's rounds, and the run's of them
+  const int p0 = (int)max((int64_t)0, r0 - t0), p1 = (int)min((int64_t)nr, r1 - t0);
+  const int f = max(p0, run * A.run), e = min(p1, (run + 1) * A.run);
   if (f >= e) return false;
   const int tiles = a4_tiles(s), first = (int)(s.row0 % KV4_TILE);
-  job->nch = (int)max((int64_t)0, min(e, (int64_t)tiles) - f);
+  job->nch = max(0, min(e, tiles) - f);
   job->own = s.ok != nullptr && e == tiles;
   const int64_t at = h * A.head_bytes + (s.row0 / KV4_TILE + f) * kv4_tile_bytes(HD);
   job->k = s.k + at;
@@ -492,10 +515,12 @@ __device__ __forceinline__ bool a4_job(const A4Args &A, int64_t i, A4Job *job) {
   job->ov = s.ok ? s.ov + (int64_t)h * kv4_tile_bytes(HD) : nullptr;
   job->b = b;
   job->h = h;
-  job->lo = (int)(f * KV4_TILE) - first;
+  job->lo = (int)((int64_t)f * KV4_TILE - first);
   job->n = s.n;
   job->whole = f == 0 && e == nr && !A.always_part;
-  job->slot = (int64_t)blockIdx.x + pair;
+  job->prior = f > p0;
+  job->left = (p1 - e + A.run - 1) / A.run;
+  job->slot = (int64_t)blockIdx.x + (int64_t)b * A.kv + h;
   return true;
 }
 
@@ -610,13 +635,13 @@ __global__ void __launch_bounds__(A4<HD, NQ, SPL>::THREADS, 1) k_attn4(const __g
   tc_fence_after();
   const uint32_t tb = tslot;
 
-  // The next window of up to A4_JOBS pieces (after the first, once every warp is done
+  // The next window of up to A4_JOBS runs (after the first, once every warp is done
   // with the last one): how many there are (fewer in the CTA's last window). Every warp asks for
   // the same windows, in its own loop.
-  auto window = [&](int64_t i0) {
+  auto window = [&](int64_t i0, auto makes) {
     if (i0 == 0) return njobs;
     __syncthreads();
-    if (warp == 0) {
+    if (decltype(makes)::value && warp == 0) {
       const bool have = lane < A4_JOBS && a4_job<HD>(A, i0 + lane, jobs + lane);
       const uint32_t m = __ballot_sync(0xffffffffu, have);
       if (lane == 0) njobs = __popc(m);
@@ -640,7 +665,7 @@ __global__ void __launch_bounds__(A4<HD, NQ, SPL>::THREADS, 1) k_attn4(const __g
     // the groups run through a piece's chunks on their own
     const int group_bar = 2 + (warp >> 2);
     for (int64_t i0 = 0; nj == A4_JOBS; i0 += A4_JOBS) {
-    nj = window(i0);
+    nj = window(i0, std::true_type{});
     for (int ji = 0; ji < nj; ++ji) {
       const A4Job &job = jobs[ji];
       const int nch = job.nch;
@@ -651,7 +676,7 @@ __global__ void __launch_bounds__(A4<HD, NQ, SPL>::THREADS, 1) k_attn4(const __g
       for (int i = 0; i < QPT; ++i) l[i] = 0.f;
       if (lane < QPT) nm[lane] = A4_NONE;
       if (nch > 0) {
-        stage_q(job);  // (the scores of the piece before, the last ones' last readers, are done)
+        if (!job.prior) stage_q(job);  // (the scores of the piece before, the last ones' last readers, are done)
         warp_arrive(qfull);
       }
       // the queries' factors are written; the last piece's sums have been read
@@ -873,6 +898,8 @@ __global__ void __launch_bounds__(A4<HD, NQ, SPL>::THREADS, 1) k_attn4(const __g
       }
       const int d = key;  // this thread's dimension of O
       const bool stat = (warp & 3) == 0 && lane < QPT && q0 + lane < Q;  // this lane writes query q0 + lane's statistics
+      float *part = A.part + (job.slot * Q + q0) * (HD + 4);
+      const int at = HD + job.left % 2 * 2, before = HD + 2 - job.left % 2 * 2;  // this run's and the last one's statistics
       float m = -INFINITY, L = 0.f;
       if (stat && have && nm[lane] != A4_NONE) {
         const float4 s = *(const float4 *)lsum[q0 + lane];
@@ -881,15 +908,30 @@ __global__ void __launch_bounds__(A4<HD, NQ, SPL>::THREADS, 1) k_attn4(const __g
       }
       // (a query that has seen no row has P and so O of 0)
       if (!job.whole) {
-        float *out = A.part + (job.slot * Q + q0) * (HD + 4);
+        if (job.prior) {
+          // the runs before it, in the slot: a lane a query, then every thread its values of O
+          const float mb = lane < QPT && q0 + lane < Q ? part[lane * (HD + 4) + before] : -INFINITY;
+          const float mi = lane < QPT && have && nm[lane] != A4_NONE ? -nm[lane] : -INFINITY, M = a4_max(mi, mb);
+          const float fi = mi != -INFINITY ? a4_ex2(mi - M) : 0.f;
+          const float fb = mb != -INFINITY ? a4_ex2(mb - M) : 0.f;
+          if (stat) {
+            m = M;
+            L = fmaf(part[lane * (HD + 4) + before + 1], fb, L * fi);
+          }
+#pragma unroll
+          for (int i = 0; i < QPT; ++i) {
+            const float a = __shfl_sync(0xffffffffu, fi, i), b = __shfl_sync(0xffffffffu, fb, i);
+            if (d < HD && q0 + i < Q) o[i] = fmaf(part[i * (HD + 4) + d], b, o[i] * a);
+          }
+        }
         if (stat) {
-          out[lane * (HD + 4) + HD] = m;
-          out[lane * (HD + 4) + HD + 1] = L;
+          part[lane * (HD + 4) + at] = m;
+          part[lane * (HD + 4) + at + 1] = L;
         }
         if (d < HD) {
 #pragma unroll
           for (int i = 0; i < QPT; ++i)
-            if (q0 + i < Q) out[i * (HD + 4) + d] = o[i];
+            if (q0 + i < Q) part[i * (HD + 4) + d] = o[i];
         }
       } else {
         const int64_t row0 = (int64_t)job.b * R * A.heads + job.h * rep;
@@ -922,7 +964,7 @@ __global__ void __launch_bounds__(A4<HD, NQ, SPL>::THREADS, 1) k_attn4(const __g
     const int key = (warp & 3) * 32 + lane;
     const uint32_t lrow = (uint32_t)((warp & 3) * 32) << 16;
     for (int64_t i0 = 0; nj == A4_JOBS; i0 += A4_JOBS) {
-    nj = window(i0);
+    nj = window(i0, std::false_type{});
     int end = J;
     for (int i = 0; i < nj; ++i) end += jobs[i].nch;
     // this thread's key of the ring's stages: copied, waited for and read by it alone
@@ -1004,7 +1046,7 @@ __global__ void __launch_bounds__(A4<HD, NQ, SPL>::THREADS, 1) k_attn4(const __g
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     const int w = warp - (SMW + 8), par = w & 1;
     for (int64_t i0 = 0; nj == A4_JOBS; i0 += A4_JOBS) {
-    nj = window(i0);
+    nj = window(i0, std::false_type{});
     for (int ji = 0; ji < nj && ok && lane == 0; ++ji) {
       const A4Job &job = jobs[ji];
       const int nch = job.nch;
@@ -1175,7 +1217,7 @@ __global__ void __launch_bounds__(Few<HD>::THREADS, few_ctas(NT)) k_attn4_few(co
     const int b = P.b, h = P.h;
     const A4Seq &Sq = A.seq[b];
     const int n = Sq.n, first = (int)(Sq.row0 % KV4_TILE);
-    // the piece's groups of 16 rows, counted from row0's tile on; group ng: the own rows'
+    // the run's groups of 16 rows, counted from row0's tile on; group ng: the own rows'
     const int ng = n > 0 ? (int)(((int64_t)first + n + 15) / 16) : first / 16;
     const int s0 = first / 16 + 8 * P.r0, send = min(ng + (Sq.ok ? 1 : 0), first / 16 + 8 * P.r1);
     const int s1 = min(ng, send);
@@ -1458,7 +1500,7 @@ __global__ void __launch_bounds__(Few<HD>::THREADS, few_ctas(NT)) k_attn4_few(co
     if (P.rnd >= P.rend) pdl_trigger();
     __syncthreads();
     constexpr int V4 = HD / 4;
-    const bool whole = P.whole(A);
+    const bool whole = P.r0 == 0 && P.r1 == P.nr && !A.always_part;
     const int64_t slot0 = P.slot(A);
     for (int id = threadIdx.x; id < Q * V4; id += Few<HD>::THREADS) {
       const int q = id / V4, d = id % V4 * 4;
@@ -1482,10 +1524,24 @@ __global__ void __launch_bounds__(Few<HD>::THREADS, few_ctas(NT)) k_attn4_few(co
       }
       if (!whole) {
         float *out = A.part + (slot0 * Q + q) * (HD + 4);
+        const int left = P.left();
+        if (P.r0 > P.begin(A)) {
+          // the runs before, in the slot (their statistics in two places in turn, a piece's
+          // last ones where the merge reads them)
+          const float Mb = out[HD + 2 - left % 2 * 2], Lb = out[HD + 3 - left % 2 * 2], Mi = M;
+          const float4 x = *(const float4 *)(out + d);
+          M = a4_max(M, Mb);
+          const float fi = seen ? a4_ex2(Mi - M) : 0.f, fb = Mb != -INFINITY ? a4_ex2(Mb - M) : 0.f;
+          L = fmaf(Lb, fb, L * fi);
+          acc.x = fmaf(x.x, fb, acc.x * fi);
+          acc.y = fmaf(x.y, fb, acc.y * fi);
+          acc.z = fmaf(x.z, fb, acc.z * fi);
+          acc.w = fmaf(x.w, fb, acc.w * fi);
+        }
         *(float4 *)(out + d) = acc;
         if (d == 0) {
-          out[HD] = M;
-          out[HD + 1] = L;
+          out[HD + left % 2 * 2] = M;
+          out[HD + 1 + left % 2 * 2] = L;
         }
       } else {
         const int64_t row = ((int64_t)b * R + q % R) * A.heads + h * rep + q / R;
@@ -1501,8 +1557,8 @@ __global__ void __launch_bounds__(Few<HD>::THREADS, few_ctas(NT)) k_attn4_few(co
 }
 
 // y of a query row from its pair's partials (m in base 2), one warp a row; a row
-// that no piece saw anything of is 0 (lse -inf). A pair that one CTA took whole is
-// written already. PACK: the row as hi/lo planes into the output projection's
+// that no piece saw anything of is 0 (lse -inf). A pair that one CTA took whole in one run
+// is written already. PACK: the row as hi/lo planes into the output projection's
 // token tiles; the blocks past `work` clear that GEMM's outputs when it splits.
 // NB: twice as many partials are asked for before the first is needed. 8 while the
 // launch is one wave (three CTAs an SM then): a divided pair of a single sequence has
@@ -1526,7 +1582,7 @@ __global__ void __launch_bounds__(128) k_attn4_merge(const __grid_constant__ A4A
   const int nr = a4_rounds<FEW>(A.seq[b]);
   const int64_t t0 = A.round0[b] + (int64_t)g * nr;
   const int64_t i0 = a4_cta(A, t0), i1 = a4_cta(A, t0 + nr - 1);
-  if (i0 == i1 && !A.always_part) return;
+  if (i0 == i1 && nr <= A.run && !A.always_part) return;
   const int ns = (int)(i1 - i0 + 1);
   const float *base = A.part + ((i0 + (int64_t)b * A.kv + g) * Q + qi) * (HD + 4);
   float v[2][NB][DL];
@@ -1645,12 +1701,16 @@ static bool takes_few(int Q, int hd, int dtype) { return Q <= 16 || (Q <= 32 && 
 constexpr int A4_MIN_ROUNDS = 4;
 // Share the rounds out over at most `slots` CTAs; true if no pair is divided.
 template <bool FEW>
-static bool share_out(A4Args &A, int batch, int64_t slots) {
+static bool share_out(A4Args &A, int batch, int hd, int64_t slots) {
   A.batch = batch;
+  // (a round is a step of each warp of k_attn4_few, and 8 steps of k_attn4, whose chunks take
+  // two accumulators in turn where its columns leave room)
+  A.run = FEW ? A4_STEPS : A.dtype == DFLASH_F32 && (hd == 64 || A.heads / A.kv * A.R > 32) ? A4_STEPS / 8 : A4_STEPS / 4;
   int64_t most = 1;
   for (int i = 0; i < batch; ++i) {
     const int nr = a4_rounds<FEW>(A.seq[i]);
     A.round0[i + 1] = A.round0[i] + (int64_t)nr * A.kv;
+    A.run0[i + 1] = A.run0[i] + (int64_t)a4_runs(A, nr) * A.kv;
     most = std::max<int64_t>(most, nr);
   }
   const int64_t T = A.round0[batch], pairs = (int64_t)batch * A.kv;
@@ -1677,11 +1737,11 @@ static cudaError_t launch_rows(A4Args &A, int batch, int hd, int num_sms, bool &
   const int Q = A.heads / A.kv * A.R;
   few = takes_few(Q, hd, A.dtype);
   if (few) {
-    whole = share_out<true>(A, batch, (int64_t)few_ctas(Q <= 8 ? 1 : Q <= 16 ? 2 : 4) * num_sms);
+    whole = share_out<true>(A, batch, hd, (int64_t)few_ctas(Q <= 8 ? 1 : Q <= 16 ? 2 : 4) * num_sms);
     if (A.dtype == DFLASH_F32) return hd == 128 ? launch_few_hd<128, 2>(A, st) : launch_few_hd<64, 2>(A, st);
     return hd == 128 ? launch_few_hd<128, 1>(A, st) : launch_few_hd<64, 1>(A, st);
   }
-  whole = share_out<false>(A, batch, num_sms);
+  whole = share_out<false>(A, batch, hd, num_sms);
   return hd == 128 ? launch_a4_hd<128>(A, st) : launch_a4_hd<64>(A, st);
 }
 // The rows of A, and the merge of divided pairs.

@@ -2,7 +2,7 @@
 import pytest
 
 torch = pytest.importorskip("torch")
-from test_kv4 import DT, _attend_case, _cache, on_gpu, quantise  # noqa: E402
+from test_kv4 import DT, _attend_case, _cache, attend, on_gpu, quantise, tolerance  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -79,3 +79,70 @@ def test_attention_of_large_random_scores_stays_among_the_values(dtype, hd, R, h
         assert bool((y.abs() <= top).all())
         # no row's weights have vanished: a mean of values of +-1 and more is not 0 everywhere
         assert bool((y.abs().amax(-1) > 0).all())
+
+
+@on_gpu
+@pytest.mark.parametrize("dtype,hd,R,rep,n", [("f32", 128, 16, 2, 1 << 17), ("f32", 128, 32, 2, 1 << 17), ("f32", 64, 48, 1, 1 << 17),
+                                              ("f16", 128, 16, 3, 1 << 19), ("f32", 64, 4, 2, 1 << 20), ("f32", 128, 16, 1, 1 << 19)])
+@pytest.mark.parametrize("flat", [True, False])
+def test_attention_sums_do_not_drift_over_many_rows(dtype, hd, R, rep, n, flat):
+    """160 pairs of 131,072 rows and more, some CTA's piece as long: the error does not grow with the rows.
+    A sum stays in the matrix instructions for 256 of their steps at most, each of which may cut off 2^-22 of
+    it (2^-23 of the sum so far, as much of the products beside it): twice what the tolerance has a step for.
+    Flat: equal scores and values. Else: scores that swing by 40 along the rows, so that the references move
+    within the runs and between them."""
+    kv = 160
+    g = torch.Generator().manual_seed(R)
+    k, v = torch.zeros(1, n, 1, hd), torch.full((1, n, 1, hd), 1.75)
+    q = torch.randn(1, R, rep, hd, generator=g)
+    if not flat:
+        at = torch.arange(n) * (2 * 3.14159 / 50000)
+        k[0, :, 0, 0], k[0, :, 0, 1] = at.sin(), at.cos()
+        phase = torch.rand(R, rep, generator=g) * 6.28
+        q[0, :, :, 0], q[0, :, :, 1] = 20 * hd ** 0.5 * phase.cos(), 20 * hd ** 0.5 * phase.sin()
+        v = torch.randn(1, n, 1, hd, generator=g) + 1
+    q = q.to(DT[dtype])
+    one = _cache(1, n, 1, hd)
+    one.write([0], k.cuda(), v.cuda())
+    c = _cache(1, n, kv, hd)
+    c.k.copy_(one.k.expand_as(c.k))
+    c.v.copy_(one.v.expand_as(c.v))
+    y = c.attend(q.unsqueeze(2).expand(1, R, kv, rep, hd).reshape(1, R, kv * rep, hd).cuda(), [0], [n], [n])
+    hk, hv = (t[:, 0].cuda().double() for t in (quantise(k)[0], quantise(v)[0]))
+    p = torch.softmax(torch.einsum("rhd,nd->rhn", q[0].cuda().double(), hk) * hd ** -0.5, -1)
+    want, bound = p @ hv, (p @ hv.abs()).amax(-1)
+    tol = tolerance(dtype, hd, 2 * 16 * 256, bound.cpu(), want.cpu()).cuda()
+    err = (y.view(R, kv, rep, hd).double() - want.unsqueeze(1)).abs().amax(-1)
+    assert bool((err <= tol.unsqueeze(1)).all()), float((err / tol.unsqueeze(1)).max())
+
+
+@on_gpu
+@pytest.mark.parametrize("dtype,hd,R,rep", [("f32", 128, 32, 2), ("f32", 128, 16, 2), ("f32", 64, 2, 1), ("f16", 64, 9, 4)])
+def test_attention_of_long_and_short_pairs_together(dtype, hd, R, rep):
+    """480 pairs of 100,000, 333, none and 20,000 rows, all from inside a tile, so that a CTA's pieces are of
+    one run or several, whole and divided, one after another; causal, and the same bits every time."""
+    kv, lo, hi = 120, [5, 1000, 40, 129], [100005, 1333, 40, 20129]
+    g = torch.Generator().manual_seed(hd + R)
+    n = max(hi)
+    k, v = (torch.randn(4, n, 1, hd, generator=g) for _ in range(2))
+    q = torch.randn(4, R, rep, hd, generator=g).to(DT[dtype])
+    one = _cache(4, n, 1, hd)
+    one.write([0] * 4, k.cuda(), v.cuda())
+    c = _cache(4, n, kv, hd)
+    c.k.copy_(one.k.expand_as(c.k))
+    c.v.copy_(one.v.expand_as(c.v))
+    args = (q.unsqueeze(2).expand(4, R, kv, rep, hd).reshape(4, R, kv * rep, hd).cuda(), lo, hi, [x - R for x in hi])
+    args[3][2] = 0
+    y, lse = c.attend(*args, causal=True, lse=True)
+    y2 = c.attend(*args, causal=True)
+    assert torch.equal(y, y2)
+    y, lse = y.view(4, R, kv, rep, hd).cpu().double(), lse.view(4, R, kv, rep).cpu().double()
+    for b in range(4):
+        ry, rl, bound = attend(q[b], quantise(k[b]), quantise(v[b]), lo[b], hi[b], args[3][b], 0, True, hd ** -0.5)
+        tol = tolerance(dtype, hd, min(hi[b] - lo[b], 2 * 16 * 256), bound, ry)
+        assert bool(((y[b] - ry.unsqueeze(1)).abs().amax(-1) <= tol.unsqueeze(1)).all()), b
+        if hi[b] > lo[b]:
+            # a thread adds up at most 256 weights of a run, and the runs are joined in f32
+            assert bool(((lse[b] - rl.unsqueeze(1)).abs() <= (hd + 8 + 300) * 2.0 ** -22 + 2.0 ** -22 * rl.abs().max()).all())
+        else:
+            assert bool((lse[b] == float("-inf")).all()) and bool((y[b] == 0).all())
