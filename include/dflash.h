@@ -228,9 +228,13 @@ int dflash_kv4_read(int32_t batch, int32_t kv_heads, int32_t head_dim, int64_t r
  * i * q_seq_stride + r * q_row_stride elements on, [heads][head_dim]
  * contiguous; y is [batch][q_rows][heads][head_dim] of the same type, lse (or
  * NULL) f32 [batch][q_rows][heads]: the natural logarithm of the softmax's sum
- * (-infinity for a row that sees nothing). f32 rows keep about 22 bits through
- * the products; f16 and bf16 rows enter exactly and the weights are rounded to
- * f16 (2^-12 of each). heads / kv_heads * q_rows <= 64. y may be q's own memory
+ * (-infinity for a row that sees nothing). f32 rows and their weights p_t enter
+ * the products as two f16 each (about 22 bits); f16 and bf16 rows enter as they
+ * are, with the weights rounded to f16 (2^-12 of each). What is below 2^-35 of a
+ * row's largest value is lost to f16's lowest step, and of a weight what is below
+ * 2^-34 of the largest of the rows taken together with it (8,192 at most). Sums
+ * are f32, in the matrix instructions for at most 256 of their steps, each of
+ * which may cut off 2^-22 of the sum. heads / kv_heads * q_rows <= 64. y may be q's own memory
  * when q is laid out as y is. The workspace is
  * 16-byte aligned and holds dflash_kv4_attention_workspace_bytes bytes (0 for
  * sizes the library does not take); calls that overlap on the GPU need one

@@ -197,7 +197,13 @@ __global__ void __launch_bounds__(256) k_kv4_read(const __grid_constant__ Kv4Seq
 // for every piece, and a second kernel merges a pair's partials. (With a fixed number
 // of splits a pair, 32 blocks over 8,192 rows each took 190 us and not 153: the last
 // CTAs of a launch had the GPU to themselves.)
-constexpr float A4_TAU = 11.f, A4_BIAS = 4.f;
+// Weights 2^(x - m) stay at or below 2^TAU, inside f16's range, and a new reference puts
+// the row's largest weight so far at 2^BIAS: high, because what a weight's f16 form (or
+// its two planes) loses to f16's lowest step is then at most 2^-34 of the largest. (With
+// 2^4, weights 20 nats below the largest had lost a sixth of themselves, and those from
+// 29 bits below on all.) TAU - BIAS is what scores may grow by before the reference has
+// to follow: 5.9 bits cost nothing against 7, 3.9 bits 2 - 15% of a launch.
+constexpr float A4_TAU = 15.9f, A4_BIAS = 10.f;
 constexpr float A4_NONE = 3.402823466e38f;  // minus the reference of a query that has seen no row
 
 // A matrix instruction cuts off what its f32 sum does not hold, always towards 0, so that
@@ -408,7 +414,7 @@ __device__ __forceinline__ float a4_max(float a, float b) {
 //
 // The softmax runs in base 2 with a lazy reference: P = 2^(x - m) with m moved
 // only when a score passes it by more than TAU (then m is the largest score so
-// far less BIAS), so that P stays below 2^(TAU + BIAS) in f16. Scores are per
+// far less BIAS), so that P stays at 2^TAU or below in f16. Scores are per
 // key, so finding a new reference reduces over lanes; a chunk in which no score
 // passes costs one barrier with a vote. A query that has seen no row yet has
 // f32's lowest number as its reference, which any score passes. A score that is not a number

@@ -146,3 +146,33 @@ def test_attention_of_long_and_short_pairs_together(dtype, hd, R, rep):
             assert bool(((lse[b] - rl.unsqueeze(1)).abs() <= (hd + 8 + 300) * 2.0 ** -22 + 2.0 ** -22 * rl.abs().max()).all())
         else:
             assert bool((lse[b] == float("-inf")).all()) and bool((y[b] == 0).all())
+
+
+@on_gpu
+@pytest.mark.parametrize("dtype,hd,R,rep", [("f32", 128, 4, 1), ("f32", 128, 16, 1), ("f32", 64, 16, 2), ("f32", 128, 16, 2),
+                                            ("f32", 128, 32, 2), ("f32", 64, 48, 1), ("bf16", 128, 1, 4), ("f16", 128, 16, 2),
+                                            ("bf16", 64, 16, 4)])
+@pytest.mark.parametrize("spike", [0, 16500])
+def test_attention_keeps_a_long_tail_under_one_large_weight(dtype, hd, R, rep, spike):
+    """One row 12 to 24 nats above 32,768 equal ones, whose values alone are not 0: the output is the tail's
+    share. A weight enters the products to 2^-34 of the largest of its run at worst, and a run has at most
+    8,192 rows, so beside the tolerance the output may be off by 2^-34 of the value for each of those. 320
+    pairs, so that a CTA has a pair or more and full runs meet the one row's reference."""
+    n, kv, batch, V = 32769, 160, 2, 1.75                      # 7 * 0.25: held exactly
+    k, v = torch.zeros(1, n, 1, hd), torch.full((1, n, 1, hd), V)
+    k[0, spike] = V
+    v[0, spike] = 0
+    one = _cache(1, n, 1, hd)
+    one.write([0], k.cuda(), v.cuda())
+    c = _cache(batch, n, kv, hd)
+    c.k.copy_(one.k.expand_as(c.k))
+    c.v.copy_(one.v.expand_as(c.v))
+    gap = torch.linspace(12, 24, R * rep).view(R, 1, rep, 1)
+    q = (gap / (V * hd ** 0.5)).expand(R, kv, rep, hd).reshape(1, R, kv * rep, hd).expand(batch, -1, -1, -1).to(DT[dtype])
+    y = c.attend(q.cuda(), [0] * batch, [n] * batch, [n] * batch).cpu().double()
+    s = q[0, :, :rep].double().sum(-1) * V * hd ** -0.5         # the large score; the others are 0
+    w = (n - 1) * torch.exp(-s)
+    want = (V * w / (1 + w)).view(1, R, 1, rep, 1)
+    tol = tolerance(dtype, hd, n, want[..., 0], want) + 8192 * 2.0 ** -34 * V
+    err = (y.view(batch, R, kv, rep, hd) - want).abs().amax(-1)
+    assert bool((err <= tol).all()), float((err / tol).max())
