@@ -680,6 +680,7 @@ __global__ void __launch_bounds__(A4<HD, NQ, SPL>::THREADS, 1) k_attn4(const __g
       float l[QPT];
 #pragma unroll
       for (int i = 0; i < QPT; ++i) l[i] = 0.f;
+      __syncwarp();  // the warp's lanes have read the references of the piece before
       if (lane < QPT) nm[lane] = A4_NONE;
       if (nch > 0) {
         if (!job.prior) stage_q(job);  // (the scores of the piece before, the last ones' last readers, are done)

@@ -176,3 +176,15 @@ def test_attention_keeps_a_long_tail_under_one_large_weight(dtype, hd, R, rep, s
     tol = tolerance(dtype, hd, n, want[..., 0], want) + 8192 * 2.0 ** -34 * V
     err = (y.view(batch, R, kv, rep, hd) - want).abs().amax(-1)
     assert bool((err <= tol).all()), float((err / tol).max())
+
+
+@on_gpu
+@pytest.mark.parametrize("dtype,R", [("f32", 17), ("bf16", 48)])
+def test_attention_of_pairs_that_see_nothing_between_others(dtype, R):
+    """2,560 pairs of one tile each, a CTA's many pieces taking turns between ranges that are empty, seen by the
+    last query rows only, and full: every query's reference starts over with its piece."""
+    hi = [(0, 100, 128)[b % 3] for b in range(64)]
+    anchor = [(0, 128, 127)[b % 3] for b in range(64)]
+    lo = [(0, 60, 0)[b % 3] for b in range(64)]
+    y = _attend_case(dtype, 64, R, 40, 40, 128, 128, lo, hi, anchor, window=40 + R)
+    assert bool((y[0] == 0).all()) and bool((y[2] != 0).any())
