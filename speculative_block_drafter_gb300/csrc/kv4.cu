@@ -693,7 +693,7 @@ __global__ void __launch_bounds__(A4<HD, NQ, SPL>::THREADS, 1) k_attn4(const __g
         const int j = J + i, sb = j & 1, u = j >> 1;
         const bool is_own = i == own_i;
         const int lo = first + i * KV4_TILE;  // the chunk's first row in the range
-        const bool edge = is_own || lo < va || lo + KV4_TILE > vb;
+        const bool edge = is_own || lo < va || vb - lo < KV4_TILE;  // (lo + 128 can pass 2^31)
         ok = ok && mbar_wait_warp(sfull + 8 * sb, u & 1);
         tc_fence_after();
         // scores in the base-2 domain, raw or against the reference
@@ -1469,7 +1469,7 @@ __global__ void __launch_bounds__(Few<HD>::THREADS, few_ctas(NT)) k_attn4_few(co
       if (s + (S - 1) * W < s1) fetch((slot + S - 1) % S);
       cp_async_commit();
       const int lo = s * 16 - first;
-      step(lo, n, lo < va || lo + 16 > vb, false, slot * F::STAGE);
+      step(lo, n, lo < va || vb - lo < 16, false, slot * F::STAGE);  // (lo + 16 can pass 2^31)
       slot = (slot + 1) % S;
     }
     cp_async_wait<0>();

@@ -2,7 +2,7 @@
 import pytest
 
 torch = pytest.importorskip("torch")
-from test_kv4 import DT, _attend_case, _cache, attend, on_gpu, quantise, tolerance  # noqa: E402
+from test_kv4 import DT, _attend_case, _cache, _lib, attend, on_gpu, quantise, tolerance  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -188,3 +188,34 @@ def test_attention_of_pairs_that_see_nothing_between_others(dtype, R):
     lo = [(0, 60, 0)[b % 3] for b in range(64)]
     y = _attend_case(dtype, 64, R, 40, 40, 128, 128, lo, hi, anchor, window=40 + R)
     assert bool((y[0] == 0).all()) and bool((y[2] != 0).any())
+
+
+@on_gpu
+@pytest.mark.parametrize("R", [1, 48])
+def test_attention_over_the_longest_cache(R):
+    """A cache of 2^31 - 1 rows, whose last tile's last row is not one of them: all rows alike, at a score of
+    about -100, so that a row read past the end (a score of 0) would take all the weight. K and V are one buffer
+    of 77 GB."""
+    L = _lib()
+    rows, hd = (1 << 31) - 1, 64
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 100 GB of device memory")
+    nb = L.dflash_kv4_cache_bytes(1, hd, rows)
+    from speculative_block_drafter_gb300.drafter import kv4_values
+    c = torch.full((nb,), 0x18, dtype=torch.uint8, device="cuda")     # codes of 0 and -7, scales of eight bits
+    x = kv4_values(c[:128 * (hd // 2 + hd // 16)].view(1, -1), hd)[0]
+    q = torch.full((1, R, 1, hd), -100 * hd ** 0.5 / float(x.sum()), device="cuda")
+    y, lse = torch.empty_like(q), torch.empty(1, R, 1, device="cuda")
+    wb = L.dflash_kv4_attention_workspace_bytes(1, R, 1, 1, hd)
+    ws = torch.empty(wb, dtype=torch.uint8, device="cuda")
+    L.dflash_kv4_attention(1, R, 1, 1, hd, rows, L.pointers([c.data_ptr()]), L.pointers([c.data_ptr()]), L.int64s([0]),
+                           L.int64s([rows]), L.int64s([rows]), 0, 0, hd ** -0.5, q.data_ptr(), R * hd, hd, 0,
+                           y.data_ptr(), lse.data_ptr(), ws.data_ptr(), wb,
+                           torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    del c
+    torch.cuda.empty_cache()
+    assert L.dflash_device_error(reset=True) == 0
+    # a run's sums are off by 256 steps of 2^-22, joined in f32 in 3,449 runs of a CTA and 152 partials
+    assert bool(((y - x).abs() <= (256 * 2.0 ** -22 + 3601 * 2.0 ** -24) * x.abs()).all())
+    assert bool((lse - (torch.log(torch.tensor(float(rows))).item() - 100)).abs().max() < 1e-3)
