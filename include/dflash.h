@@ -450,12 +450,14 @@ int dflash_select_sample(const float *logits, const float *hp, const uint32_t *a
  * A logit of -inf or NaN has probability 0; among logits of +inf p is shared; a
  * row without any probability keeps no token and gives the token 0xFFFFFFFF.
  * Writes accepted i32 [batch] (drafts kept) and tokens u32 [batch][k + 1]: the
- * kept drafts, the next token, then 0xFFFFFFFF. The draw carries the weights to
- * 2^-39 of the largest, as whole numbers. k 0..255 (0: a token is drawn from
- * the target alone), vocab 1..2,097,152, batch * (k + 1) <= 65,535. The
- * workspace is 16-byte aligned and holds dflash_verify_workspace_bytes bytes (0
- * for sizes the library does not take); calls that overlap on the GPU need one
- * each. Errors: ARG, CAPACITY, CUDA. */
+ * kept drafts, the next token, then 0xFFFFFFFF. p is carried to 2^-39 of the
+ * row's largest, as whole numbers, for the verdict and for the draw, so that both
+ * are the same wherever the rows lie (a token below 2^-41 of the largest has
+ * none). k 0..255 (0: a token is drawn from the target alone), vocab
+ * 1..2,097,152, batch * (k + 1) <= 65,535. The workspace is 16-byte aligned and
+ * holds dflash_verify_workspace_bytes bytes (0 for sizes the library does not
+ * take); calls that overlap on the GPU need one each. Errors: ARG, CAPACITY,
+ * CUDA. */
 size_t dflash_verify_workspace_bytes(int32_t batch, int32_t k, int32_t vocab);
 int dflash_verify(int32_t batch, int32_t k, int32_t vocab, const void *logits, int32_t dtype, int64_t ld,
                   const uint32_t *drafted, const int32_t *n_drafted, const uint32_t *cand, const float *cand_q,

@@ -41,6 +41,7 @@ constexpr int VF_RUN = VF_CHUNK / (VS_THREADS / 32);  // of a warp: a run, whose
 constexpr int VF_TOP = 32;
 constexpr int VF_ROWS = 256;     // rows of a sequence (k + 1)
 constexpr uint32_t VF_NONE = 0xFFFFFFFFu;
+constexpr int VF_OPEN = -1;
 
 struct VfArgs {
   const void *logits;
@@ -223,13 +224,29 @@ __device__ __forceinline__ unsigned long long vf_warp_sum(unsigned long long v) 
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-// u q Z 2^40 < w, the left side to about 2^-46.
-__device__ __forceinline__ bool vf_below(float u, float q, float Z, unsigned long long w) {
+// u q Z 2^40 < w: 1 or 0, or -1 where Z, a sum of f32 exponentials, does not tell. Z is
+// within 2^-16 of the sum of the row's whole-number weights: exponents are off by 2^-22 of
+// up to 21 that matter, their powers by 2^-22 in each of three steps, the sums by 32
+// roundings, and the weights by 1.5 of 2^40 for each of up to 2^21.
+__device__ __forceinline__ int vf_below(float u, float q, float Z, unsigned long long w) {
   const float p = u * q, pe = fmaf(u, q, -p);
   const float z = p * Z, ze = fmaf(p, Z, -z) + pe * Z;
   const float wh = __ull2float_rn(w), wl = __ll2float_rn((long long)(w - __float2ull_rn(wh)));
   const float sc = (float)(1ull << FX_BITS);
-  return (z * sc - wh) + (ze * sc - wl) < 0.f;
+  const float d = (z * sc - wh) + (ze * sc - wl);
+  return w > 0ull && fabsf(d) <= z * sc * 0x1p-16f ? -1 : d < 0.f;
+}
+// u q Z < w of whole numbers w <= Z, exactly.
+__device__ bool vf_less(float u, float q, unsigned long long Z, unsigned long long w) {
+  if (!(u * q < 2.f)) return false;  // (nor where it is not a number)
+  if (!(u > 0.f && q > 0.f)) return w > 0ull;
+  const int bu = __float_as_int(u), bq = __float_as_int(q), eu = bu >> 23, eq = bq >> 23;
+  const unsigned long long m = (unsigned long long)(eu ? (bu & 0x7fffff) | 0x800000 : bu) *
+                               (unsigned long long)(eq ? (bq & 0x7fffff) | 0x800000 : bq);
+  const int sh = 300 - (eu ? eu : 1) - (eq ? eq : 1);  // u q = m 2^-sh, m < 2^48
+  if (w == 0ull || sh < 0) return false;
+  if (64 - __clzll((long long)w) + sh > 127) return true;  // m Z < 2^110
+  return (unsigned __int128)m * Z < (unsigned __int128)w << sh;
 }
 
 template <typename T>
@@ -237,10 +254,14 @@ __global__ void __launch_bounds__(VS_THREADS, 2) k_verify_sample(const __grid_co
   constexpr int W = VS_THREADS / 32, PER = VF_RUN / 32;
   __shared__ unsigned long long tab[64], red[W], sub[VS_THREADS], taken, base, target;
   __shared__ float rowm[VF_ROWS];
-  __shared__ int rowi[VF_ROWS];
-  __shared__ int kept, last, pick, owner;
+  __shared__ int rowi[VF_ROWS];    // greedy: the largest value's index; else VF_OPEN where not decided
+  __shared__ float rowq[VF_ROWS];
+  __shared__ int kept, last, pick, owner, open;
   if (threadIdx.x < 64) tab[threadIdx.x] = kFxTable[threadIdx.x];
-  if (threadIdx.x == 64) kept = A.k;
+  if (threadIdx.x == 64) {
+    kept = A.k;
+    open = INT_MAX;
+  }
   sub[threadIdx.x] = 0ull;
   __syncthreads();
   const int b = blockIdx.y, chunk = blockIdx.x, t = threadIdx.x, warp = t >> 5, lane = t & 31;
@@ -295,14 +316,38 @@ __global__ void __launch_bounds__(VS_THREADS, 2) k_verify_sample(const __grid_co
       rowm[r] = M;
       rowi[r] = at;
       if (r < n) {
-        const bool keep =
+        const int keep =
             greedy ? M > -INFINITY && x == (uint32_t)at : vf_below(u, q, Z, fx_weight(l, M, sc, tab));
-        if (!keep) atomicMin(&kept, r);
+        if (keep < 0) {
+          rowi[r] = VF_OPEN;
+          rowq[r] = q;
+          atomicMin(&open, r);
+        }
+        if (keep == 0) atomicMin(&kept, r);
       }
     }
   }
   if (greedy && chunk > 0) return;
   __syncthreads();
+  // rows too near their border for Z (one in 30,000 and fewer) are summed in whole numbers,
+  // by all threads, in the rows' order
+  for (int r = open; r < min(kept, n); ++r) {
+    if (greedy || rowi[r] != VF_OPEN) continue;
+    const T *lo = (const T *)A.logits + ((int64_t)b * K1 + r) * A.ld;
+    const float m = rowm[r];
+    unsigned long long s = 0ull;
+    for (int e = t; e < A.vocab; e += VS_THREADS) s += fx_weight(vf_value(lo[e]), m, sc, tab);
+    s = vf_warp_sum(s);
+    if (lane == 0) red[warp] = s;
+    __syncthreads();
+    if (t == 0) {
+      s = 0ull;
+      for (int w = 0; w < W; ++w) s += red[w];
+      const float l = vf_value(lo[A.drafted[(int64_t)b * A.k + r]]);  // (a token of the vocabulary: its weight is not 0)
+      if (!vf_less(A.u[(int64_t)b * K1 + r], rowq[r], s, fx_weight(l, m, sc, tab))) kept = r;
+    }
+    __syncthreads();
+  }
   const int a = min(kept, n);      // drafts kept; the token is drawn from row a
   const float M = rowm[a];
   const T *lr = (const T *)A.logits + ((int64_t)b * K1 + a) * A.ld;
