@@ -411,13 +411,16 @@ int dflash_select_static(const float *logits, const float *hp, const uint32_t *a
  * selector's order, whose cumulative probability is above the row's uniform
  * number. Pointers and sizes as dflash_select_static, and
  *   temperature  f32 [batch] (device), or NULL for 1; T that is not above 0: the
- *                first highest score with probability 1 (the selector's choice)
+ *                first highest score with probability 1 (the selector's choice,
+ *                but where its f32 scores do not tell two candidates apart)
  *   uniforms     f32 [batch][k] in [0, 1) (device)
  *   chosen       u32 [batch][k]; cand u32 and cand_q f32 [batch][k][top]: every
  *                row's candidates and their probabilities, the proposal that
  *                dflash_verify takes.
- * Scores and cumulative probabilities are carried to about 2^-39, so that the
- * choice is that of exact arithmetic. An anchor token >= vocab gives tokens of
+ * Scores are sums of exact products, off by about 2^-43 of their terms' sizes
+ * (rank^2 2^-48 at worst), cumulative probabilities are carried to 2^-39, so that
+ * the choice is that of exact arithmetic but for uniform numbers that near a
+ * border. An anchor token >= vocab gives tokens of
  * 0xFFFFFFFF and probabilities of 0. The workspace is 16-byte aligned and holds
  * dflash_select_sample_workspace_bytes bytes (0 for sizes the library does not
  * take). Errors: ARG, CAPACITY, CUDA. */

@@ -51,7 +51,7 @@ __device__ __forceinline__ FxScale fx_scale(float T) {
   return s;
 }
 
-// The weight of a difference d + e <= 0 (d, e: an unevaluated sum); 0 for NaN. Without
+// The weight of a difference d + e <= 0 (an unevaluated sum, e at most a step of d); 0 for NaN. Without
 // branches, so that several run side by side: below 2^-42 (and for NaN) y is -42, whose
 // weight rounds to 0 whatever the low parts hold then (their part is below 2^-14).
 // `tab`: kFxTable, in shared memory.

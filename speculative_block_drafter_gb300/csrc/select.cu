@@ -372,9 +372,10 @@ cudaError_t select_tokens(const float *logits, const float *hp, const uint32_t *
 //   stage 4 (one CTA per sequence): the chain, a table look-up a row.
 // 480 rows of 151,936 (top 16, rank 64): 82 us, of which stage 1 some 48 (HBM: 292 MB),
 // stage 2 and 3 15 - 20 each; 15 rows: 16 us, four launches of some 4 us of latency.
-// The scores are sums of exact products kept as two floats (a sum of 64 terms
-// is then off by about 2^-44 of them): a choice turns on a border between two
-// cumulative weights, and an f32 score would move it by 2^-20.
+// The scores are sums of exact products kept as two floats (a sum of n terms is then
+// off by n^2 2^-48 of their sizes at worst: 2^-36 for 64, where 2^-43 is usual): a
+// choice turns on a border between two cumulative weights, and an f32 score would move
+// it by 2^-20.
 struct SampleScratch {
   unsigned long long *cmax, *cands;
   float *q;       // [rows][top predecessors][top candidates]
@@ -506,8 +507,12 @@ __global__ void __launch_bounds__(ROW_THREADS) k_row_sample(
     } else if (mh == INFINITY) {
       w = h == INFINITY ? 1ull : 0ull;
     } else if (h > -INFINITY) {     // (lanes past the candidates hold -inf)
-      const float d = h - mh, b = d - h;
-      const float e = (h - (d - b)) + (-mh - b) + (l - ml);
+      float d = h - mh;
+      const float b = d - h;
+      float e = (h - (d - b)) + (-mh - b) + (l - ml);
+      const float r = d + e;        // (where h and mh are near, the low parts are the larger)
+      e -= r - d;
+      d = r;
       w = fx_weight_diff(d, e, fs, tab);
     }
 #pragma unroll

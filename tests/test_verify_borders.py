@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
-from test_verify import DT, _cu, on_gpu, softmax, verify  # noqa: E402
+from test_verify import DT, _cu, on_gpu, sample_chain, softmax, verify  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -63,3 +63,38 @@ def test_verify_decides_beside_the_border(dtype, V, ld, top):
         ref = verify(xf[i], d[i], u[i].astype(np.float64), float(T[i]), cand[i] if top else None, q[i] if top else None, k)
         assert (acc[i], list(tok[i])) == ref, i
     assert 0 < acc.sum() < b * k
+
+
+@on_gpu
+@pytest.mark.parametrize("rank,top", [(16, 8), (64, 16), (256, 32)])
+def test_select_sample_keeps_what_f32_scores_would_lose(rank, top):
+    """Candidates whose scores agree to an f32 step, at a temperature of a few such steps: the probabilities
+    turn on parts of the products below f32. The low part of a sum of n terms takes up n errors of 2^-24 of
+    the terms' sizes together, and adding those up in f32 costs another 2^-24 of it each time: n^2 2^-48 in all.
+    Over the temperature that is the weights' relative error, twice (the weight and the largest one), to which
+    the probabilities' own (2^-24, 2^-39) come."""
+    from speculative_block_drafter_gb300 import drafter as D
+    rng = np.random.default_rng(rank)
+    V, b = 512, 48
+    pred, succ = ((rng.standard_normal((V, rank)) / rank ** 0.25).astype(np.float16) for _ in range(2))
+    hp = rng.standard_normal((b, 1, rank)).astype(np.float32)
+    anchor = rng.integers(0, V, b)
+    logits = np.full((b, 1, V), -200.0, np.float32)
+    size = np.zeros(b)
+    for i in range(b):
+        a = pred[anchor[i]].astype(np.float64) * hp[i, 0].astype(np.float64)
+        cand = rng.permutation(V)[:top]
+        logits[i, 0, cand] = (6.0 - succ[cand].astype(np.float64) @ a).astype(np.float32)
+        size[i] = (np.abs(succ[cand].astype(np.float64)) @ np.abs(a) + np.abs(logits[i, 0, cand])).max()
+    T = np.full(b, 2.0 ** -21, np.float32)
+    u = rng.random((b, 1)).astype(np.float32)
+    _, cand, q = D.select_sample(_cu(logits), _cu(hp), _cu(anchor, torch.int32), _cu(pred), _cu(succ), top, _cu(T), _cu(u))
+    cand, q = cand.cpu().numpy(), q.cpu().numpy().astype(np.float64)
+    spread = 0
+    for i in range(b):
+        _, rcand, rq = sample_chain(logits[i], hp[i], int(anchor[i]), pred, succ, top, float(T[i]), u[i])
+        assert np.array_equal(cand[i], rcand)
+        tol = (2.0 ** -24 + 2 * rank ** 2 * 2.0 ** -48 * size[i] / T[i]) * rq + 2.0 ** -39
+        assert np.all(np.abs(q[i] - rq) <= tol), float((np.abs(q[i] - rq) / tol).max())
+        spread += (rq > 0.02).sum() > 1
+    assert spread > b / 2                                      # near ties, as they are meant to be
