@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(ROW_THREADS) k_row_sample(
         for (int i = 0; i < 2; ++i) {
           const float x = i ? pv.y : pv.x, z = i ? cv.y : cv.x, s = hs[2 * e + i];
           const float a = x * s, al = fmaf(x, s, -a);  // x s = a + al
-          const float y = a * z;
+          const float y = __fmul_rn(a, z);         // (fused into the sum below, its rounding would count twice)
           two_add(h, l, y);
           l += fmaf(a, z, -y) + al * z;
         }
