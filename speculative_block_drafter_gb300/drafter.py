@@ -295,7 +295,7 @@ class Drafter:
         w.fc = f16(weights["fc"])
         w.hidden_norm, w.norm = vec(weights["hidden_norm"]), vec(weights["norm"])
         w.sel = f16(weights["sel"])
-        self._books = [torch.from_numpy(np.ascontiguousarray(weights[n], dtype=np.float16)).to(self.dev)
+        self._books = [torch.from_numpy(np.ascontiguousarray(weights[n]).view(np.int16)).to(self.dev).view(torch.float16)
                        for n in ("pred_book", "succ_book")]
         w.pred_book, w.succ_book = keep(self._books[0]), keep(self._books[1])
         w.head = int4(weights["head"])

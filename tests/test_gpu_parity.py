@@ -525,3 +525,24 @@ def test_route_margin_matches_oracle():
     ref = np.array([O.route_margin(r, mb, Bb, mc, Bc) for r in rows])
     assert np.abs(got - ref).max() <= 2e-5 * max(1.0, np.abs(ref).max()), np.abs(got - ref).max()
     assert ref[3] > 0.5 and ref[4] < -0.5 and got[3] > 0.5 and got[4] < -0.5
+
+
+def test_codebooks_given_as_bits():
+    """The selector's codebooks as 16-bit patterns (as a file reader without f16 gives them, and as the other
+    f16 weights may come) give what their f16 arrays give."""
+    from speculative_block_drafter_gb300.drafter import Drafter
+    g = di.workload("tiny").geometry
+    w = di.make_weights(g, 0)
+    bits = dict(w, **{n: np.ascontiguousarray(w[n]).view(np.uint16) for n in ("pred_book", "succ_book")})
+    h = torch.from_numpy(di.block_rows(g, 0, 7).astype(np.float32)).cuda().unsqueeze(0)
+    tok = torch.tensor([7], dtype=torch.int32, device="cuda")
+    u = torch.rand(1, g.block - 1, generator=torch.Generator().manual_seed(1)).cuda()
+    out, logits = [], None
+    for x in (w, bits):
+        d = Drafter(g, x, max_batch=1, ctx_cap=256)
+        if logits is None:                 # (one block's: its split sums may differ in their last bits)
+            logits, hp = d.block([0], h)
+        out.append([*d.select(logits, hp, tok), *d.select_sample(logits, hp, tok, None, u)])
+        torch.cuda.synchronize()
+        d.close()
+    assert all(torch.equal(a, b) for a, b in zip(*out))
