@@ -202,8 +202,9 @@ size_t dflash_kv4_cache_bytes(int32_t kv_heads, int32_t head_dim, int64_t rows);
  * every cache's row count. k and v are device rows of `dtype`: row t of sequence
  * i starts i * seq_stride + t * row_stride elements on and holds
  * [kv_heads][head_dim] contiguously. Other rows of the caches are left as they
- * are. n = 0 does nothing. Errors: ARG (also: one buffer as a K and a V cache,
- * two sequences writing the same rows of one cache), CAPACITY (rows past the
+ * are. n = 0 does nothing. Errors: ARG (also: a K and a V cache in one memory, two
+ * caches that overlap without being one, two sequences writing the same rows of
+ * one cache), CAPACITY (rows past the
  * cache), CUDA. */
 int dflash_kv4_write(int32_t batch, int32_t kv_heads, int32_t head_dim, int64_t rows, void *const *ctx_k,
                      void *const *ctx_v, const int64_t *at, int32_t n, const void *k, int64_t k_seq_stride,

@@ -1862,13 +1862,18 @@ int dflash_kv4_write(int32_t batch, int32_t kv_heads, int32_t head_dim, int64_t 
   for (int i = 0; i < batch; ++i) {
     if (at[i] < 0) return bad_arg(who, "a negative cache row");
     if (at[i] > rows - n) return dflash_fail(DFLASH_E_CAPACITY, "kv4_write: rows past the cache");
-    // no cache row is written twice in a call
+  }
+  // no cache row is written twice in a call: caches are apart, or one and the same
+  const int64_t bytes = (int64_t)kv_heads * head_bytes(head_dim, rows);
+  auto apart = [&](const void *a, const void *b) { return (uintptr_t)a + bytes <= (uintptr_t)b || (uintptr_t)b + bytes <= (uintptr_t)a; };
+  for (int i = 0; i < batch; ++i)
     for (int j = 0; j < batch; ++j) {
-      if (ctx_k[i] == ctx_v[j]) return bad_arg(who, "one buffer as a K and a V cache");
+      if (!apart(ctx_k[i], ctx_v[j])) return bad_arg(who, "a K and a V cache in one memory");
+      if (j < i && !apart(ctx_k[i], ctx_k[j]) && ctx_k[i] != ctx_k[j]) return bad_arg(who, "two K caches that overlap");
+      if (j < i && !apart(ctx_v[i], ctx_v[j]) && ctx_v[i] != ctx_v[j]) return bad_arg(who, "two V caches that overlap");
       if (j < i && (ctx_k[i] == ctx_k[j] || ctx_v[i] == ctx_v[j]) && at[i] < at[j] + n && at[j] < at[i] + n)
         return bad_arg(who, "two sequences write the same rows of one cache");
     }
-  }
   if (n == 0) return DFLASH_OK;
   Kv4Rows X{};
   X.p[0] = k, X.p[1] = v;
