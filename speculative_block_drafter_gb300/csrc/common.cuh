@@ -91,9 +91,10 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// Order-preserving map of a float onto u32 (larger float -> larger integer).
+// Order-preserving map of a float onto u32 (larger float -> larger integer; the two
+// zeros, which are equal, alike).
 __device__ __forceinline__ uint32_t f32_ordered(float f) {
-  uint32_t b = __float_as_uint(f);
+  uint32_t b = __float_as_uint(f + 0.f);
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 __device__ __forceinline__ float f32_from_ordered(uint32_t u) {

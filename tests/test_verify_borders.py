@@ -3,6 +3,8 @@ are known to far below a step of f32."""
 import numpy as np
 import pytest
 
+from oracle import dflash_oracle as O
+
 torch = pytest.importorskip("torch")
 from test_verify import DT, _cu, on_gpu, sample_chain, softmax, verify  # noqa: E402
 
@@ -98,3 +100,31 @@ def test_select_sample_keeps_what_f32_scores_would_lose(rank, top):
         assert np.all(np.abs(q[i] - rq) <= tol), float((np.abs(q[i] - rq) / tol).max())
         spread += (rq > 0.02).sum() > 1
     assert spread > b / 2                                      # near ties, as they are meant to be
+
+
+@on_gpu
+@pytest.mark.parametrize("zeros", [1, 30, 3000])
+def test_selectors_take_the_two_zeros_as_equal(zeros):
+    """Rows whose largest logits are zeros of both signs: equal values, so the lower index first, within a chunk
+    of the rows, across chunks and past what a candidate list holds."""
+    from speculative_block_drafter_gb300 import _lib as L
+    from speculative_block_drafter_gb300 import drafter as D
+    rng = np.random.default_rng(zeros)
+    b, k, V, rank, top = 3, 5, 5000, 16, 8
+    logits = -1 - rng.random((b, k, V)).astype(np.float32)
+    for row in logits.reshape(-1, V):
+        row[rng.permutation(V)[:zeros]] = np.where(rng.random(zeros) < 0.5, 0.0, -0.0)
+    pred, succ = ((rng.standard_normal((V, rank)) / 4).astype(np.float16) for _ in range(2))
+    hp = rng.standard_normal((b, k, rank)).astype(np.float32)
+    anchor = rng.integers(0, V, b)
+    u = rng.random((b, k)).astype(np.float32)
+    t = [_cu(logits), _cu(hp), _cu(anchor, torch.int32), _cu(pred), _cu(succ)]
+    ch, cand, _ = D.select_sample(*t, top, None, _cu(u))
+    best, plain = (torch.empty(b, k, dtype=torch.int32, device="cuda") for _ in range(2))
+    L.dflash_select_static(*(x.data_ptr() for x in t), b, k, V, V, rank, top, best.data_ptr(), plain.data_ptr(),
+                           torch.cuda.current_stream().cuda_stream)
+    for i in range(b):
+        rc, rcand, _ = sample_chain(logits[i], hp[i], int(anchor[i]), pred, succ, top, 1.0, u[i])
+        assert np.array_equal(cand[i].cpu().numpy(), rcand) and list(ch[i].cpu().numpy()) == list(rc)
+        chosen, first = O.select_with(hp[i], logits[i], int(anchor[i]), pred, succ, top)
+        assert list(best[i].cpu().numpy()) == list(chosen) and list(plain[i].cpu().numpy()) == list(first)
