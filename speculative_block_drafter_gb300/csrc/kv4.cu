@@ -395,8 +395,8 @@ __device__ __forceinline__ float a4_max(float a, float b) {
 //   the next 4         K: thread = one key, codes -> f16 -> tensor memory
 //   the next 4         V: thread = one key, codes -> f16 -> shared memory
 //   the next 4         MMA issue, one thread each: S of even and of odd chunks,
-//                      O of even and of odd chunks (one accumulator each; a
-//                      single one and its issuer when N is 128)
+//                      O of even and of odd chunks (two accumulators each, which
+//                      halves what their sums lose; one and one issuer at N 128)
 // Chunks are counted through the CTA's pieces, so that the next piece's keys and
 // scores are under way while the last one's results are written. The softmax warps
 // stage a piece's queries. A key's codes come through a ring of stages in shared
@@ -426,7 +426,8 @@ struct A4 {
   static constexpr int SMT = 32 * SMW;
   static constexpr int THREADS = 32 * (SMW + 12);
   static constexpr int NS = NQ * SPL;                // columns of S and of O
-  static constexpr int NO = NS <= 64 ? 2 : 1;        // output accumulators
+  static constexpr int NO = NS <= 64 ? 4 : 1;        // output accumulators, taken in turn
+  static constexpr int NI = NO == 1 ? 1 : 2;         // threads that issue O's products
   static constexpr int KC = HD / 2;                  // tensor-memory columns of a K slot
   static constexpr int TK = 0, TS = 2 * KC, TO = TS + 2 * NS;
   static_assert(TO + NO * NS <= 512, "tensor memory");
@@ -547,7 +548,7 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity) {
 template <int HD, int NQ, int SPL>
 __global__ void __launch_bounds__(A4<HD, NQ, SPL>::THREADS, 1) k_attn4(const __grid_constant__ A4Args A) {
   using C = A4<HD, NQ, SPL>;
-  constexpr int QPT = C::QPT, SMW = C::SMW, NS = C::NS, NO = C::NO;
+  constexpr int QPT = C::QPT, SMW = C::SMW, NS = C::NS, NO = C::NO, NI = C::NI;
   extern __shared__ __align__(1024) uint8_t smraw[];
   uint8_t *sm = smraw + ((1024 - (smem_u32(smraw) & 1023)) & 1023);
   const uint32_t smb = smem_u32(sm);
@@ -576,7 +577,7 @@ __global__ void __launch_bounds__(A4<HD, NQ, SPL>::THREADS, 1) k_attn4(const __g
       mbar_init(pvdone + 8 * i, 1);
     }
     mbar_init(qfull, SMW);
-    mbar_init(fin, 2 + NO);
+    mbar_init(fin, 2 + NI);
     mbar_fence_init();
     dead[0] = dead[1] = dead[2] = dead[3] = 0;
   }
@@ -801,10 +802,10 @@ __global__ void __launch_bounds__(A4<HD, NQ, SPL>::THREADS, 1) k_attn4(const __g
             if (any && ok) {  // alike in every lane
 #pragma unroll
               for (int o = 0; o < NO; ++o)
-                if (o < i) {  // chunk j - 1's accumulator, then chunk j - 2's
+                if (o < i) {  // chunk j - 1's accumulator, then those of the chunks before
 #pragma unroll
                   for (int p = 0; p < SPL; ++p) {
-                    const uint32_t col = tb + lrow + C::TO + (NO == 2 ? (j - 1 - o) & 1 : 0) * NS + p * NQ + q0;
+                    const uint32_t col = tb + lrow + C::TO + ((j - 1 - o) & (NO - 1)) * NS + p * NQ + q0;
                     uint32_t v[QPT];
                     tmem_ld_n<QPT>(col, v);
                     tc_wait_ld();
@@ -892,7 +893,7 @@ __global__ void __launch_bounds__(A4<HD, NQ, SPL>::THREADS, 1) k_attn4(const __g
 #pragma unroll
             for (int p = 0; p < SPL; ++p) {
               uint32_t v[QPT];
-              tmem_ld_n<QPT>(tb + lrow + C::TO + (NO == 2 ? (J - 1 - a) & 1 : 0) * NS + p * NQ + q0, v);
+              tmem_ld_n<QPT>(tb + lrow + C::TO + ((J - 1 - a) & (NO - 1)) * NS + p * NQ + q0, v);
               tc_wait_ld();
 #pragma unroll
               for (int i = 0; i < QPT; ++i) o[i] += __uint_as_float(v[i]);
@@ -1073,10 +1074,10 @@ __global__ void __launch_bounds__(A4<HD, NQ, SPL>::THREADS, 1) k_attn4(const __g
                    sw128_desc(qb + (ks >> 2) * C::QB + (ks & 3) * 32), idesc, ks > 0);
           mma_commit(sfull + 8 * par);
         }
-      } else if (w - 2 < NO) {
+      } else if (w - 2 < NI) {
         // A (V) and B (P) both MN-major
         constexpr uint32_t idesc = f16_idesc(128, NS) | (1u << 15) | (1u << 16);
-        for (int i = NO == 2 ? (J ^ par) & 1 : 0; i < nch; i += NO) {
+        for (int i = NI == 2 ? (J ^ par) & 1 : 0; i < nch; i += NI) {
           const int j = J + i, sb = j & 1, u = j >> 1;
           if (!(ok = mbar_wait(vfull + 8 * sb, u & 1))) break;
           // P written: by then every softmax thread has read the pieces before out of O
@@ -1085,7 +1086,7 @@ __global__ void __launch_bounds__(A4<HD, NQ, SPL>::THREADS, 1) k_attn4(const __g
           const bool is_own = job.own && i == nch - 1;
           const int lo = job.lo + i * KV4_TILE;
           const int ka = is_own ? 0 : max(0, -lo), kb = is_own ? R : min(KV4_TILE, job.n - lo);
-          const uint32_t acc = tb + C::TO + (NO == 2 ? par : 0) * NS;
+          const uint32_t acc = tb + C::TO + (j & (NO - 1)) * NS;
           const uint32_t vb = smb + sb * C::VST, pb = smb + C::OFF_P + sb * C::PST;
           // only the steps of 16 keys that hold a row
           for (int ks = ka / 16; ks < (kb + 15) / 16; ++ks)
@@ -1100,7 +1101,7 @@ __global__ void __launch_bounds__(A4<HD, NQ, SPL>::THREADS, 1) k_attn4(const __g
     __syncwarp();
     }
   }
-  if (lane == 0 && warp >= SMW + 8 && warp - (SMW + 8) < 2 + NO) {
+  if (lane == 0 && warp >= SMW + 8 && warp - (SMW + 8) < 2 + NI) {
     // every MMA of this thread completed before the tensor memory is freed
     mma_commit(fin);
     mbar_wait(fin, 0);
