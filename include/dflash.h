@@ -202,9 +202,10 @@ size_t dflash_kv4_cache_bytes(int32_t kv_heads, int32_t head_dim, int64_t rows);
  * every cache's row count. k and v are device rows of `dtype`: row t of sequence
  * i starts i * seq_stride + t * row_stride elements on and holds
  * [kv_heads][head_dim] contiguously. Other rows of the caches are left as they
- * are. n = 0 does nothing. Errors: ARG (also: a K and a V cache in one memory, two
- * caches that overlap without being one, two sequences writing the same rows of
- * one cache), CAPACITY (rows past the
+ * are. n = 0 does nothing. Host arrays, here and below, are read during the call:
+ * a launch captured into a graph repeats the rows it was captured with. Errors: ARG
+ * (also: a K and a V cache in one memory, two caches that overlap without being
+ * one, two sequences writing the same rows of one cache), CAPACITY (rows past the
  * cache), CUDA. */
 int dflash_kv4_write(int32_t batch, int32_t kv_heads, int32_t head_dim, int64_t rows, void *const *ctx_k,
                      void *const *ctx_v, const int64_t *at, int32_t n, const void *k, int64_t k_seq_stride,
@@ -235,11 +236,11 @@ int dflash_kv4_read(int32_t batch, int32_t kv_heads, int32_t head_dim, int64_t r
  * row's largest value is lost to f16's lowest step, and of a weight what is below
  * 2^-34 of the largest of the rows taken together with it (8,192 at most). Sums
  * are f32, in the matrix instructions for at most 256 of their steps, each of
- * which may cut off 2^-22 of the sum. heads / kv_heads * q_rows <= 64. y may be q's own memory
- * when q is laid out as y is. The workspace is
- * 16-byte aligned and holds dflash_kv4_attention_workspace_bytes bytes (0 for
- * sizes the library does not take); calls that overlap on the GPU need one
- * each. Errors: ARG, CAPACITY (rows past the cache, workspace), CUDA. */
+ * which may cut off 2^-22 of the sum. heads / kv_heads * q_rows <= 64. y may be
+ * q's own memory when q is laid out as y is. The workspace is 16-byte aligned and
+ * holds dflash_kv4_attention_workspace_bytes bytes (0 for sizes the library does
+ * not take); calls that overlap on the GPU need one each. Errors: ARG, CAPACITY
+ * (rows past the cache, workspace), CUDA. */
 size_t dflash_kv4_attention_workspace_bytes(int32_t batch, int32_t q_rows, int32_t heads, int32_t kv_heads,
                                             int32_t head_dim);
 int dflash_kv4_attention(int32_t batch, int32_t q_rows, int32_t heads, int32_t kv_heads, int32_t head_dim,

@@ -210,7 +210,7 @@ constexpr float A4_NONE = 3.402823466e38f;  // minus the reference of a query th
 // a sum of n / 16 steps drifts by some 2^-23 of itself a step (3e-4 after 32,768 rows). A
 // long piece is therefore taken in runs of at most 256 steps of a sum, whose results are
 // joined in ordinary f32 in the piece's slot. (A run's end and the next one's start cost
-// k_attn4 about 2.5 us: 32 blocks over 32,768 rows each 533 us, in one run a piece 516.)
+// k_attn4 about 2.5 us: 32 blocks over 32,768 rows each 529 us, in one run a piece 516.)
 constexpr int A4_STEPS = 256;
 
 struct A4Seq {
@@ -402,15 +402,17 @@ __device__ __forceinline__ float a4_max(float a, float b) {
 // stage a piece's queries. A key's codes come through a ring of stages in shared
 // memory that its thread alone fills (asynchronous copies) and reads.
 //
-// What bounds it: no one part. An MMA of M 128 and K 16 takes 120 - 180 cycles
-// whatever its N, so a chunk's 16 take some 2,200, where HBM brings a chunk in 784;
-// a softmax turn of 8 queries a thread takes as long (16 queries: 3,600), mostly in
-// its steps from one wait, load or vote to the next, and a CTA's first chunk, last
-// results and the merge about 10 us that nothing covers. (Leaving out three quarters
-// of the MMAs, or the dequantisation, or the exponentials each shortens a launch by
-// 2 - 10%; two chunks a turn, or packed f32 operations, by nothing.) 32 f32 blocks of 16 over
-// up to 8,192 rows each (8 KV heads of 128, 2 queries a head): 135 us, the merge
-// included, for 282 MB; one block over 32,768 rows (4 queries a head): 39 us.
+// What bounds it: no one part. A chunk takes some 2,200 cycles (with 16 queries a softmax
+// thread 3,600), where HBM brings it in 784. The tensor pipe is 19 - 23% active: one
+// thread issues an MMA in 50 - 70 cycles (N 32 to 128 alike, on an idle SM), and the last
+// one's results are there some 240 cycles later, so that a chunk's eight of S take 810
+// cycles and its eight of O 890, beside other chunks'. A softmax turn is mostly its steps
+// from one wait, load or vote to the next, and a CTA's first chunk, last results and the
+// merge are about 10 us that nothing covers. (Leaving out three quarters of the MMAs, or
+// the dequantisation, or the exponentials each shortens a launch by 2 - 10%; two chunks a
+// turn, or packed f32 operations, by nothing.) 32 f32 blocks of 16 over up to 8,192 rows
+// each (8 KV heads of 128, 2 queries a head): 140 us, the merge included, for 282 MB; one
+// block over 32,768 rows (4 queries a head): 43 us.
 //
 // The softmax runs in base 2 with a lazy reference: P = 2^(x - m) with m moved
 // only when a score passes it by more than TAU (then m is the largest score so
@@ -1117,11 +1119,11 @@ __global__ void __launch_bounds__(A4<HD, NQ, SPL>::THREADS, 1) k_attn4(const __g
 
 // ---------------------------------------------------------------- few query rows
 //
-// A tcgen05.mma of M 128 takes 120 - 180 cycles whatever its N, so that 128 keys
-// cost k_attn4 some 2,200 cycles where HBM brings them in 784. Up to 32
-// columns (queries, or twice the queries with hi and lo planes) mma.sync m16n8k16
-// (2 cycles an SM each) is cheaper, and its operands are registers: the codes go
-// from global memory through a thread's registers into the fragments.
+// k_attn4 takes some 2,200 cycles for 128 keys, however few the queries, where HBM
+// brings them in 784. Up to 32 columns (queries, or twice the queries with hi and lo
+// planes) mma.sync m16n8k16 (2 cycles an SM each) is cheaper, and its operands are
+// registers: the codes go from global memory through a thread's registers into the
+// fragments.
 //   S^T (16 keys x 8 queries) = K Q^T, O^T (16 values x 8 queries) += V^T P^T
 // with K and V as the A operands. The orders of the contraction (head dimension;
 // keys) and of the output's rows are free, so the fragments are laid over the
@@ -1139,7 +1141,7 @@ __global__ void __launch_bounds__(A4<HD, NQ, SPL>::THREADS, 1) k_attn4(const __g
 // the codes one group ahead in registers instead, the warps waited for memory
 // 40% of their time). What bounds it is the issue of instructions, 66% of the slots,
 // and the pipe that the products share with the dequantisation: 32 tokens over 8,192
-// rows each (8 KV heads of 128, 4 queries a head, bf16) take 60 us for 282 MB, 4.7
+// rows each (8 KV heads of 128, 4 queries a head, bf16) take 63 us for 282 MB, 4.5
 // TB/s. The groups of 32 values are 272
 // (K) and 320 (V) bytes apart in a stage, which keeps the reads free of bank
 // conflicts. No warp waits for another until the CTA joins its warps' results.
@@ -1711,8 +1713,8 @@ constexpr int A4_MIN_ROUNDS = 4;
 template <bool FEW>
 static bool share_out(A4Args &A, int batch, int hd, int64_t slots) {
   A.batch = batch;
-  // (a round is a step of each warp of k_attn4_few, and 8 steps of k_attn4, whose chunks take
-  // two accumulators in turn where its columns leave room)
+  // a round is a step of each warp of k_attn4_few, and 8 steps of k_attn4, whose chunks take
+  // four accumulators in turn where there is room (128 steps of each in 64 chunks)
   A.run = FEW ? A4_STEPS : A.dtype == DFLASH_F32 && (hd == 64 || A.heads / A.kv * A.R > 32) ? A4_STEPS / 8 : A4_STEPS / 4;
   int64_t most = 1;
   for (int i = 0; i < batch; ++i) {
@@ -1752,7 +1754,7 @@ static cudaError_t launch_rows(A4Args &A, int batch, int hd, int num_sms, bool &
   whole = share_out<false>(A, batch, hd, num_sms);
   return hd == 128 ? launch_a4_hd<128>(A, st) : launch_a4_hd<64>(A, st);
 }
-// The rows of A, and the merge of divided pairs.
+// The rows of A, and the merge of divided pairs (and of those of several runs).
 static cudaError_t attend(A4Args &A, int batch, int hd, int num_sms, cudaStream_t st) {
   bool few, whole;
   const cudaError_t e = launch_rows(A, batch, hd, num_sms, few, whole, st);

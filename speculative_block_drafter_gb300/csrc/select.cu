@@ -51,8 +51,8 @@ static size_t row_scratch(int width, int top) {
 size_t select_scratch_bytes(int max_rows, int width, int top) { return (size_t)max_rows * row_scratch(width, top) + 256; }
 
 
-// Eight logits of a row from `idx` on (those past the row: -inf, of which no key is
-// made), as two vectors where the row's start allows it.
+// Eight logits of a row from `idx` on, as two vectors where the row's start allows it
+// (0 for those past the row: the caller looks at the index before it makes a key).
 __device__ __forceinline__ void load_logits8(const float *__restrict__ lr, int idx, int width, float (&x)[8]) {
   if (idx + 8 <= width && ((uintptr_t)(lr + idx) & 15) == 0) {
     const float4 a = __ldg((const float4 *)(lr + idx)), b = __ldg((const float4 *)(lr + idx) + 1);
@@ -370,8 +370,8 @@ cudaError_t select_tokens(const float *logits, const float *hp, const uint32_t *
 //   A warp takes a predecessor, a lane a candidate (up to 16 candidates: half a
 //   lane's products each); cumulative weights are whole numbers (fixed.cuh).
 //   stage 4 (one CTA per sequence): the chain, a table look-up a row.
-// 480 rows of 151,936 (top 16, rank 64): 82 us, of which stage 1 some 48 (HBM: 292 MB),
-// stage 2 and 3 15 - 20 each; 15 rows: 16 us, four launches of some 4 us of latency.
+// 480 rows of 151,936 (top 16, rank 64): 83 us, of which stage 1 some 48 (HBM: 292 MB),
+// stage 2 and 3 15 - 20 each; 15 rows: 17 us, four launches of some 4 us of latency.
 // The scores are sums of exact products kept as two floats (a sum of n terms is then
 // off by n^2 2^-48 of their sizes at worst: 2^-36 for 64, where 2^-43 is usual): a
 // choice turns on a border between two cumulative weights, and an f32 score would move
